@@ -7,7 +7,7 @@ namespace e3gb {
 
 __device__ __forceinline__ uint32_t shared_address(const void* p) { return uint32_t(__cvta_generic_to_shared(p)); }
 
-// BYTES bytes, or zeros where `live` is false (nothing is read then)
+// BYTES bytes, or zeros where `live` is false (nothing is read then). Both addresses are multiples of BYTES either way.
 template <int BYTES>
 __device__ __forceinline__ void copy_async(void* dst, const void* src, bool live = true) {
     const int n = live ? BYTES : 0;

@@ -160,9 +160,12 @@ struct Ring {
     using R = RawT<T, VEC>;
     static constexpr int kBytes = int(sizeof(R)) * NV * THREADS;
 
-    // row: its first entry. Vectors past the last one read as zero.
+    // row: its first entry. Vectors past the last one read as zero: their copies read nothing, but have a source
+    // address all the same, which has to be aligned. A tensor of ODD rows may begin inside a vector; that
+    // vector's start is in the same 16 bytes of memory as the tensor's.
     static __device__ __forceinline__ void fetch(char* slot, const Tensor<T>& t, const T* row,
                                                  const Layout<VEC, L, NV, ODD>& y, bool live) {
+        const T* nothing = ODD ? reinterpret_cast<const T*>(reinterpret_cast<uintptr_t>(t.at) & ~uintptr_t(sizeof(R) - 1)) : t.at;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             R* to = reinterpret_cast<R*>(slot) + j * THREADS + threadIdx.x;
@@ -175,7 +178,7 @@ struct Ring {
                     continue;
                 }
             }
-            copy_async<sizeof(R)>(to, ok ? from : t.at, ok);
+            copy_async<sizeof(R)>(to, ok ? from : nothing, ok);
         }
     }
     static __device__ __forceinline__ R get(const char* slot, int j) {

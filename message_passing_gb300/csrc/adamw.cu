@@ -162,10 +162,12 @@ __device__ __forceinline__ float max_or_nan(float a, float b) {
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
     return m;
 }
-// root and reciprocal are the units' approximations, each within one unit in the last place
+// Root and reciprocal are the units' approximations, each within two units of 2^-24 relative. The root takes
+// subnormal numbers as they are: a v of 1e-40 (gradients of 1e-19) taken for zero would leave eps alone
+// under m. The reciprocal's operand is a normal number, at least eps >= 1e-30.
 __device__ __forceinline__ float update(float p, float m, float v, float keep, const AdamwRates& r) {
     float root, quotient;
-    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(root) : "f"(v));
+    asm("sqrt.approx.f32 %0, %1;" : "=f"(root) : "f"(v));
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(quotient) : "f"(fmaf(root, r.root, r.eps)));
     return fmaf(p, keep, -(m * quotient * r.step_size));
 }

@@ -1,0 +1,32 @@
+"""AdamW's update of the parameters where single roundings decide: tiny gradients, small weight decay.
+
+u = 2^-24. The update lr m / (1 - beta1^t) / (sqrt(v / (1 - beta2^t)) + eps), from moments rounded to fp32, takes
+a root and a reciprocal within 2 u each and at most eight further roundings: 12 u of it.
+"""
+import numpy as np
+import pytest
+import torch
+
+import message_passing_gb300 as e3
+import oracle
+from gpu_util import to_np
+from test_gpu_adamw import U, _normal
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("offset", [0, 1])
+@pytest.mark.parametrize("eps", [1e-8, 1e-18, 1e-20, 1e-30])
+def test_adamw_of_tiny_gradients(cuda, bits, offset, eps):
+    """The second moment of gradients below 1e-17 is a subnormal number, and still what the step is divided by."""
+    g = torch.logspace(-19, -15, 3000, device="cuda") * torch.sign(_normal(3000, 4))
+    g = torch.cat([g.new_zeros(offset), g])[offset:]
+    p = _normal(3000, 5, offset=offset)
+    opt = e3.AdamW.create([p], weight_decay=0.0, state_bits=bits)
+    before, zero = to_np(p), np.zeros(3000)
+    e3.adamw_step(opt, [g], lr=1e-2, step=1, eps=eps)
+    want, m, v = oracle.adamw.step(before, to_np(g), zero, zero, lr=1e-2, t=1, eps=eps, dtype=np.float32)
+    assert np.all(v > 0) and np.any(v < 1e-38)
+    size = 1e-2 * np.abs(m) / 0.1 / (np.sqrt(v.astype(np.float64) / 0.001) + eps)
+    assert np.all(np.abs(to_np(p) - want) <= U * np.abs(want) + 12 * U * size)

@@ -165,11 +165,19 @@ __device__ __forceinline__ float max_or_nan(float a, float b) {
 // Root and reciprocal are the units' approximations, each within two units of 2^-24 relative. The root takes
 // subnormal numbers as they are: a v of 1e-40 (gradients of 1e-19) taken for zero would leave eps alone
 // under m. The reciprocal's operand is a normal number, at least eps >= 1e-30.
-__device__ __forceinline__ float update(float p, float m, float v, float keep, const AdamwRates& r) {
+__device__ __forceinline__ float update(float p, float m, float v, float2 keep, const AdamwRates& r) {
     float root, quotient;
     asm("sqrt.approx.f32 %0, %1;" : "=f"(root) : "f"(v));
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(quotient) : "f"(fmaf(root, r.root, r.eps)));
-    return fmaf(p, keep, -(m * quotient * r.step_size));
+    return fmaf(p, keep.x, fmaf(p, keep.y, -(m * quotient * r.step_size)));
+}
+
+// 1 - lr wd as the sum of two fp32 numbers: one of them would round an lr wd of 1e-7 to 1.2e-7 and one of 2e-8
+// to nothing, at every step the same way.
+__device__ __forceinline__ float2 keeps(float lr, float decay) {
+    const float d = __fmul_rn(lr, decay), rest = fmaf(lr, decay, -d);
+    const float hi = __fsub_rn(1.f, d), t = __fsub_rn(hi, 1.f);
+    return make_float2(hi, __fsub_rn(__fsub_rn(__fsub_rn(1.f, __fsub_rn(hi, t)), __fadd_rn(d, t)), rest));
 }
 
 // four entries of m and v (8-bit codes) in units of their block's scales; both formats are subsets
@@ -255,7 +263,7 @@ template <class TG>
 struct Block8 {
     // the exponent fields of the new scales come back in m_field and v_field
     static __device__ __forceinline__ void step(const Stage<TG>& in, float m_scale, float v_scale, float* at_p,
-                                                __nv_bfloat16* at_copy, int64_t s, float keep, const AdamwState& st,
+                                                __nv_bfloat16* at_copy, int64_t s, float2 keep, const AdamwState& st,
                                                 const AdamwRates& r, float clip, uint32_t& m_field, uint32_t& v_field) {
         const int lane = threadIdx.x & 31;
         // m_scale is a power of two: code (m_scale beta1) is (code m_scale) beta1, bit for bit
@@ -342,7 +350,7 @@ struct Block8 {
 // The same for a tensor's last, shorter block and for tensors without vector alignment: entry by entry.
 template <class TG>
 __device__ __noinline__ void ragged_block8(const AdamwTensor& a, const TG* g, const AdamwState& st, const AdamwRates& r,
-                                           int64_t at, float clip, float keep) {
+                                           int64_t at, float clip, float2 keep) {
     const int64_t s = a.start + at;
     const int lane = threadIdx.x & 31;
     const float m_scale = st.m_scale[s / kAdamwBlock], v_scale = st.v_scale[s / kAdamwBlock];
@@ -385,7 +393,7 @@ __device__ __noinline__ void ragged_block8(const AdamwTensor& a, const TG* g, co
 // a chunk with 32-bit moments
 template <class TG>
 __device__ __forceinline__ void chunk32(const AdamwTensor& a, const TG* g, const AdamwState& st, const AdamwRates& r,
-                                        int64_t at, int n, bool vectors, float clip, float keep) {
+                                        int64_t at, int n, bool vectors, float clip, float2 keep) {
     constexpr int V = kAdamwChunk / kThreads / 4;
     float* m = static_cast<float*>(st.m) + a.start + at;
     float* v = static_cast<float*>(st.v) + a.start + at;
@@ -463,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, BITS == 8 ? 3 : 2)
               [&](const AdamwTensor& a, int t, int64_t first, int64_t last) {
         const TG* g = static_cast<const TG*>(grads.g[t - tensor0]);
         if (g == nullptr) return;
-        const float keep = fmaf(-r.lr, a.decay, 1.f);
+        const float2 keep = keeps(r.lr, a.decay);
         const bool vectors = aligned4(g) && aligned4(a.p) && aligned4(a.copy);
         if constexpr (BITS == 32) {
             for (int64_t at = first; at < last; at += kAdamwChunk)

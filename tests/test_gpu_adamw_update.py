@@ -30,3 +30,18 @@ def test_adamw_of_tiny_gradients(cuda, bits, offset, eps):
     assert np.all(v > 0) and np.any(v < 1e-38)
     size = 1e-2 * np.abs(m) / 0.1 / (np.sqrt(v.astype(np.float64) / 0.001) + eps)
     assert np.all(np.abs(to_np(p) - want) <= U * np.abs(want) + 12 * U * size)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("lr,decay", [(1e-5, 0.01), (1e-6, 0.02), (1e-3, 0.1), (0.5, 1.0), (1.0, 1.0)])
+def test_adamw_decays_by_little(cuda, bits, lr, decay):
+    """p (1 - lr wd) - update is rounded once, half a unit of the result, whatever lr wd is: the factor is held in
+    48 bits, lr and wd in 24 each, and the parts below fp32's are added to the update first."""
+    n = 20_000
+    p, g = _normal(n, 5), _normal(n, 6)
+    opt = e3.AdamW.create([p], weight_decay=decay, state_bits=bits)
+    before, zero, wd = to_np(p), np.zeros(n), float(np.float32(decay))
+    e3.adamw_step(opt, [g], lr=lr, step=1)
+    want, _, _ = oracle.adamw.step(before, to_np(g), zero, zero, lr=lr, t=1, decay=wd)
+    bound = U * np.abs(want) * (1 + 1e-6) + 16 * U * lr + 4 * U * lr * wd * np.abs(before)
+    assert np.all(np.abs(to_np(p) - want) <= bound)

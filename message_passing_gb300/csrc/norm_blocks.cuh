@@ -249,7 +249,7 @@ __device__ __forceinline__ void block_backward(const NormShape& sh, int b, int64
         for (int u = 0; u < U; ++u) {
             const int64_t n = n0 + threadIdx.x / L + u * kPerBlock;
             TO* os = dx + (n * sh.x_stride + row0);
-            const float s = st[u].y, shift = -st[u].x * st[u].y;
+            const float mu = st[u].x, s = st[u].y;
             float xh[P::kRows][CG][VEC], g[P::kRows][CG][VEC], c1 = 0.f, c2 = 0.f;
 #pragma unroll
             for (int m = 0; m < P::kRows; ++m)
@@ -259,7 +259,7 @@ __device__ __forceinline__ void block_backward(const NormShape& sh, int b, int64
                     unpack(rd[u][m][c], g[m][c]);
 #pragma unroll
                     for (int k = 0; k < VEC; ++k) {
-                        xh[m][c][k] = M == 1 ? (at.in(m, c) ? fmaf(xh[m][c][k], s, shift) : 0.f) : xh[m][c][k] * s;
+                        xh[m][c][k] = M == 1 ? (at.in(m, c) ? (xh[m][c][k] - mu) * s : 0.f) : xh[m][c][k] * s;
                         dw[c][k] = fmaf(g[m][c][k], xh[m][c][k], dw[c][k]);
                         if (M == 1) db[c][k] += g[m][c][k];
                         g[m][c][k] *= wv[c][k];

@@ -331,13 +331,13 @@ __global__ void __launch_bounds__(kThreads<L>, L > 32 || NV * VEC > 16 ? 1 : NV 
         copies_wait<S - 1>();
         const char* slot = ring + get_at * kSlot;
         const float2 st = reinterpret_cast<const float2*>(slot + X::kBytes + D::kBytes)[threadIdx.x];
-        const float s = st.y, off = -st.x * st.y;
+        const float mu = st.x, s = st.y;
         float xh[kAgain ? 1 : NV][VEC], g[kAgain ? 1 : NV][VEC], c[2] = {0.f, 0.f};
         const auto form = [&](int j, float (&xv)[VEC], float (&gv)[VEC]) {   // xh and dy of vector j
             unpack(X::get(slot, j), xv);
             unpack(D::get(slot + X::kBytes, j), gv);
 #pragma unroll
-            for (int k = 0; k < VEC; ++k) xv[k] = fmaf(xv[k], s, off);
+            for (int k = 0; k < VEC; ++k) xv[k] = (xv[k] - mu) * s;   // x s - mu s would round mu s, of a large mean
             mask(xv, lay, j);
             mask(gv, lay, j);
             if (!ODD && !lay.any(j))

@@ -54,13 +54,15 @@ cudaError_t zero_padding_edges(int64_t N, int64_t E, const int32_t* csc_ptr, con
 int grid_for(const void* kernel, int block, int64_t per_block, int64_t units, int smem) {
     if (units <= 0) return 0;
     static std::mutex mu;
-    static std::map<std::tuple<const void*, int, int>, int> resident;  // blocks per device, by kernel and smem
+    // blocks per device, by kernel, device, shared memory and threads of a block (one kernel may be launched with
+    // several, the same shared memory among them)
+    static std::map<std::tuple<const void*, int, int, int>, int> resident;
     int dev = 0;
     cudaGetDevice(&dev);
     int cap = 0;
     {
         std::lock_guard<std::mutex> lk(mu);
-        const std::tuple<const void*, int, int> key(kernel, dev, smem);
+        const std::tuple<const void*, int, int, int> key(kernel, dev, smem, block);
         auto it = resident.find(key);
         if (it == resident.end()) {
             int per_sm = 0, sms = 0;

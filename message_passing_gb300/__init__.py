@@ -616,14 +616,21 @@ def _dtype_code(name, t):
     raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
 
 
-def _f32_param(name, t, *shape):
+def _elsewhere(name, t, at):
+    where = "host memory" if at < 0 else f"cuda:{at}"
+    raise ValueError(f"{name} is on {t.device}, expected all tensors of a call in the same place ({where})")
+
+
+def _f32_param(name, t, at, *shape):
     """The address of a contiguous float32 parameter, gradient or statistics array of that shape
-    (None for None)."""
+    (None for None) on device number `at` (-1: the host)."""
     import torch
     if t is None:
         return None
     if t.dtype != torch.float32:
         raise TypeError(f"{name} must be float32")
+    if t.get_device() != at:
+        _elsewhere(name, t, at)
     if t.shape != shape:
         _shape(name, t, *shape)
     if not t.is_contiguous():
@@ -648,14 +655,24 @@ def _given(stream, *own):
     return stream.cuda_stream
 
 
-def _row_stride(name, t, R, C):
-    """Entries between the rows of t [R, C], whose rows are contiguous and do not overlap."""
+def _row_stride(name, t, at, R, C):
+    """Entries between the rows of t [R, C], whose rows are contiguous and do not overlap, on device `at`."""
+    if t.get_device() != at:
+        _elsewhere(name, t, at)
     if t.shape != (R, C):
         _shape(name, t, R, C)
     s0, s1 = t.stride()
     if (s1 != 1 and C > 1) or (s0 < C and R > 1):
         raise ValueError(f"{name}: strides {(s0, s1)}: rows must be contiguous and must not overlap")
     return s0 if R > 1 else C
+
+
+def _given_workspace(ws, at):
+    if ws.get_device() != at:
+        _elsewhere("workspace", ws, at)
+    if not ws.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return ws
 
 
 @lru_cache(maxsize=256)
@@ -671,10 +688,10 @@ def layer_norm_forward(x, weight=None, bias=None, eps: float = 1e-5, out=None, d
     import torch
     if x.dim() != 2:
         raise ValueError(f"x: shape {tuple(x.shape)}, expected (rows, channels)")
-    (R, C), dev, f = x.shape, x.device, torch.float32
-    xs, w, b = _row_stride("x", x, R, C), _f32_param("weight", weight, C), _f32_param("bias", bias, C)
+    (R, C), dev, at, f = x.shape, x.device, x.get_device(), torch.float32
+    xs, w, b = _row_stride("x", x, at, R, C), _f32_param("weight", weight, at, C), _f32_param("bias", bias, at, C)
     y = torch.empty((R, C), dtype=dtype or f, device=dev) if out is None else out
-    ys = C if out is None else _row_stride("y", out, R, C)
+    ys = C if out is None else _row_stride("y", out, at, R, C)
     xd, yd = _dtype_code("x", x), _dtype_code("y", y)
     stats = torch.empty((R, 2), dtype=f, device=dev)
     s = _current(dev) if stream is None else _given(stream, stats, y if out is None else None)
@@ -690,17 +707,20 @@ def layer_norm_backward(x, weight, stats, dy, out=None, dtype=None, params: bool
     import torch
     if x.dim() != 2:
         raise ValueError(f"x: shape {tuple(x.shape)}, expected (rows, channels)")
-    (R, C), dev, f = x.shape, x.device, torch.float32
-    xs, dys = _row_stride("x", x, R, C), _row_stride("dy", dy, R, C)
-    w, st = _f32_param("weight", weight, C), _f32_param("stats", stats, R, 2)
+    (R, C), dev, at, f = x.shape, x.device, x.get_device(), torch.float32
+    xs, dys = _row_stride("x", x, at, R, C), _row_stride("dy", dy, at, R, C)
+    w, st = _f32_param("weight", weight, at, C), _f32_param("stats", stats, at, R, 2)
     dx = torch.empty((R, C), dtype=dtype or f, device=dev) if out is None else out
-    dxs = C if out is None else _row_stride("dx", out, R, C)
+    dxs = C if out is None else _row_stride("dx", out, at, R, C)
     xd, dyd, dxd = _dtype_code("x", x), _dtype_code("dy", dy), _dtype_code("dx", dx)
     dw = db = ws = None
     pw = pb = pws = nws = 0
     if params:
         dw, db = torch.empty(C, dtype=f, device=dev), torch.empty(C, dtype=f, device=dev)
-        ws = torch.empty(_layer_norm_workspace(R, C), dtype=torch.uint8, device=dev) if workspace is None else workspace
+        if workspace is None:
+            ws = torch.empty(_layer_norm_workspace(R, C), dtype=torch.uint8, device=dev)
+        else:
+            ws = _given_workspace(workspace, at)
         pw, pb, pws, nws = dw.data_ptr(), db.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size()
     s = _current(dev) if stream is None else _given(stream, dw, db, ws if workspace is None else None,
                                                     dx if out is None else None)
@@ -737,6 +757,8 @@ def _irreps_operand(blocks, x):
 
 
 def _same_layout(name, t, x):
+    if t.get_device() != x.get_device():
+        _elsewhere(name, t, x.get_device())
     if t.shape != x.shape:
         _shape(name, t, *x.shape)
     if not t.is_contiguous():
@@ -751,9 +773,9 @@ def irreps_norm_forward(blocks, x, weight=None, bias=None, eps: float = 1e-5, ou
     [N, n_blocks, 2] = (mean or 0, 1/rms) goes to the backward. y: float32, or `dtype`."""
     import torch
     _, ir, scalars = _irreps_operand(blocks, x)
-    shape, nb, dev, f = x.shape, len(blocks), x.device, torch.float32
+    shape, nb, dev, at, f = x.shape, len(blocks), x.device, x.get_device(), torch.float32
     N, _, mul = shape
-    w, b = _f32_param("weight", weight, nb, mul), _f32_param("bias", bias, scalars, mul)
+    w, b = _f32_param("weight", weight, at, nb, mul), _f32_param("bias", bias, at, scalars, mul)
     y = torch.empty(shape, dtype=dtype or f, device=dev) if out is None else out
     if out is not None:
         _same_layout("y", y, x)
@@ -771,9 +793,9 @@ def irreps_norm_backward(blocks, x, weight, stats, dy, out=None, dtype=None, par
     forward's stats; dbias is None where there is no even scalar block. params=False: dx only."""
     import torch
     key, ir, scalars = _irreps_operand(blocks, x)
-    shape, nb, dev, f = x.shape, len(key), x.device, torch.float32
+    shape, nb, dev, at, f = x.shape, len(key), x.device, x.get_device(), torch.float32
     N, _, mul = shape
-    w, st = _f32_param("weight", weight, nb, mul), _f32_param("stats", stats, N, nb, 2)
+    w, st = _f32_param("weight", weight, at, nb, mul), _f32_param("stats", stats, at, N, nb, 2)
     _same_layout("dy", dy, x)
     dx = torch.empty(shape, dtype=dtype or f, device=dev) if out is None else out
     if out is not None:
@@ -786,7 +808,7 @@ def irreps_norm_backward(blocks, x, weight, stats, dy, out=None, dtype=None, par
         if workspace is None:
             ws = torch.empty(_irreps_norm_workspace(key, mul, N), dtype=torch.uint8, device=dev)
         else:
-            ws = workspace
+            ws = _given_workspace(workspace, at)
         pw, pws, nws = dw.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size()
         if scalars:
             db = torch.empty((scalars, mul), dtype=f, device=dev)
@@ -836,13 +858,19 @@ class AdamW:
             raise ValueError(f"{n} parameters, {len(copies)} copies, {len(decay)} weight decays")
         if not 0 <= seed < 1 << 32:
             raise ValueError("seed must fit in 32 bits")
+        at = params[0].get_device()
         for i, (p, c) in enumerate(zip(params, copies)):
-            _f32_param(f"params[{i}]", p, *p.shape)
+            _f32_param(f"params[{i}]", p, at, *p.shape)
             if c is not None:
                 if c.dtype != torch.bfloat16:
                     raise TypeError(f"copies[{i}] must be bfloat16")
+                if c.get_device() != at:
+                    _elsewhere(f"copies[{i}]", c, at)
                 _shape(f"copies[{i}]", c, *p.shape)
                 _contig(c)
+        for name, t in zip(("m", "v", "m_scale", "v_scale"), state or ()):
+            if t.get_device() != at:
+                _elsewhere(name, t, at)
         lib = load()
         ptrs = lambda ts: (ctypes.c_void_p * n)(*[None if t is None else t.data_ptr() for t in ts])  # noqa: E731
         h = ctypes.c_void_p()

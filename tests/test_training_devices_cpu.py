@@ -1,0 +1,64 @@
+"""The norm and AdamW calls take tensors of one device only: the kernels get bare addresses."""
+import os
+
+import pytest
+import torch
+
+import message_passing_gb300 as e3
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    if not os.path.exists(e3.LIB_PATH):
+        from message_passing_gb300 import build
+        build.build()
+    return e3.load()
+
+
+class _Elsewhere(torch.Tensor):
+    """A host tensor that says that it lies on device 1."""
+
+    def get_device(self):
+        return 1
+
+
+def away(*shape, dtype=torch.float32):
+    return torch.zeros(*shape, dtype=dtype).as_subclass(_Elsewhere)
+
+
+X, S, W = torch.zeros(5, 8), torch.zeros(5, 2), torch.zeros(8)
+G, GS, IR = torch.zeros(5, 4, 8), torch.zeros(5, 2, 2), [(0, 1), (1, -1)]
+LN, LNB, IN, INB = e3.layer_norm_forward, e3.layer_norm_backward, e3.irreps_norm_forward, e3.irreps_norm_backward
+
+
+@pytest.mark.parametrize("call,match", [
+    (lambda: LN(X, away(8)), "weight"),
+    (lambda: LN(X, None, away(8)), "bias"),
+    (lambda: LN(X, out=away(5, 8)), "y"),
+    (lambda: LN(away(5, 8), W), "weight"),
+    (lambda: LNB(X, away(8), S, X), "weight"),
+    (lambda: LNB(X, None, away(5, 2), X), "stats"),
+    (lambda: LNB(X, None, S, away(5, 8)), "dy"),
+    (lambda: LNB(X, None, S, X, out=away(5, 8)), "dx"),
+    (lambda: LNB(X, None, S, X, workspace=away(100_000)), "workspace"),
+    (lambda: IN(IR, G, away(2, 8)), "weight"),
+    (lambda: IN(IR, G, None, away(1, 8)), "bias"),
+    (lambda: IN(IR, G, out=away(5, 4, 8)), "y"),
+    (lambda: INB(IR, G, None, away(5, 2, 2), G), "stats"),
+    (lambda: INB(IR, G, None, GS, away(5, 4, 8)), "dy"),
+    (lambda: INB(IR, G, None, GS, G, out=away(5, 4, 8)), "dx"),
+    (lambda: INB(IR, G, None, GS, G, workspace=away(100_000)), "workspace"),
+    (lambda: e3.AdamW.create([W, away(8)]), "params"),
+    (lambda: e3.AdamW.create([W], copies=[away(8, dtype=torch.bfloat16)]), "copies"),
+    (lambda: e3.AdamW.create([W], state=(torch.zeros(256), away(256))), "v"),
+])
+def test_operands_of_another_device(call, match):
+    with pytest.raises(ValueError, match=f"{match}.* is on .*expected all tensors"):
+        call()
+
+
+@pytest.mark.parametrize("call", [lambda ws: LNB(X, None, S, X, workspace=ws),
+                                  lambda ws: INB(IR, G, None, GS, G, workspace=ws)])
+def test_a_workspace_with_gaps(call):
+    with pytest.raises(ValueError, match="workspace must be contiguous"):
+        call(torch.zeros(200_000)[::2])

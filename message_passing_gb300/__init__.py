@@ -639,11 +639,14 @@ def _f32_param(name, t, at, *shape):
 
 
 def _current(device):
-    """The device's current stream, raw."""
+    """The current stream, raw, of the tensors' device, which has to be the current one: launches go there."""
     import torch
     if device.type != "cuda":
         raise ValueError(f"tensors on {device}: expected device memory")
-    return torch._C._cuda_getCurrentRawStream(device.index)
+    here = torch._C._cuda_getDevice()
+    if device.index != here:
+        raise ValueError(f"tensors on {device}, but the current device is cuda:{here}")
+    return torch._C._cuda_getCurrentRawStream(here)
 
 
 def _given(stream, *own):

@@ -1,5 +1,6 @@
 """The norm and AdamW calls take tensors of one device only: the kernels get bare addresses."""
 import os
+from types import SimpleNamespace
 
 import pytest
 import torch
@@ -62,3 +63,14 @@ def test_operands_of_another_device(call, match):
 def test_a_workspace_with_gaps(call):
     with pytest.raises(ValueError, match="workspace must be contiguous"):
         call(torch.zeros(200_000)[::2])
+
+
+def test_the_device_has_to_be_the_current_one(monkeypatch):
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: 100 + index, raising=False)
+    device = lambda i: SimpleNamespace(type="cuda", index=i)  # noqa: E731
+    assert e3._current(device(0)) == 100
+    with pytest.raises(ValueError, match="current device is cuda:0"):
+        e3._current(device(1))
+    with pytest.raises(ValueError, match="expected device memory"):
+        e3._current(torch.device("cpu"))

@@ -649,13 +649,18 @@ def _current(device):
     return torch._C._cuda_getCurrentRawStream(here)
 
 
-def _given(stream, *own):
-    """A given stream, raw. Tensors that the call allocated are marked as used there: the allocator
-    would otherwise hand them out again on the stream they were allocated on."""
-    for t in own:
-        if t is not None and t.is_cuda:
-            t.record_stream(stream)
-    return stream.cuda_stream
+def _on(stream, call, *args, out=None):
+    """call(*args) with `stream` as the current one. What the call allocates then belongs to that stream (memory
+    that went back to the caller's stream may still be in use there), and the results are kept from reuse until
+    the caller's stream is done with them too."""
+    import torch
+    caller = torch.cuda.current_stream(stream.device)
+    with torch.cuda.stream(stream):
+        results = call(*args)
+    for t in results:
+        if t is not None and t is not out:
+            t.record_stream(caller)
+    return results
 
 
 def _row_stride(name, t, at, R, C):
@@ -689,6 +694,8 @@ def layer_norm_forward(x, weight=None, bias=None, eps: float = 1e-5, out=None, d
     rstd), which the backward takes. weight, bias: float32 [C] or None. x: float32 or bfloat16; y:
     float32, or `dtype`."""
     import torch
+    if stream is not None:
+        return _on(stream, layer_norm_forward, x, weight, bias, eps, out, dtype, out=out)
     if x.dim() != 2:
         raise ValueError(f"x: shape {tuple(x.shape)}, expected (rows, channels)")
     (R, C), dev, at, f = x.shape, x.device, x.get_device(), torch.float32
@@ -697,9 +704,8 @@ def layer_norm_forward(x, weight=None, bias=None, eps: float = 1e-5, out=None, d
     ys = C if out is None else _row_stride("y", out, at, R, C)
     xd, yd = _dtype_code("x", x), _dtype_code("y", y)
     stats = torch.empty((R, 2), dtype=f, device=dev)
-    s = _current(dev) if stream is None else _given(stream, stats, y if out is None else None)
     _check((_lib or load()).e3gb_layer_norm_forward(R, C, x.data_ptr(), xs, xd, w, b, eps, y.data_ptr(), ys, yd,
-                                                    stats.data_ptr(), s))
+                                                    stats.data_ptr(), _current(dev)))
     return y, stats
 
 
@@ -708,6 +714,8 @@ def layer_norm_backward(x, weight, stats, dy, out=None, dtype=None, params: bool
     stats. dx: float32, or `dtype`; dweight, dbias: float32 [C] (with params=False: None, and only dx
     is computed)."""
     import torch
+    if stream is not None:
+        return _on(stream, layer_norm_backward, x, weight, stats, dy, out, dtype, params, workspace, out=out)
     if x.dim() != 2:
         raise ValueError(f"x: shape {tuple(x.shape)}, expected (rows, channels)")
     (R, C), dev, at, f = x.shape, x.device, x.get_device(), torch.float32
@@ -725,10 +733,8 @@ def layer_norm_backward(x, weight, stats, dy, out=None, dtype=None, params: bool
         else:
             ws = _given_workspace(workspace, at)
         pw, pb, pws, nws = dw.data_ptr(), db.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size()
-    s = _current(dev) if stream is None else _given(stream, dw, db, ws if workspace is None else None,
-                                                    dx if out is None else None)
     _check((_lib or load()).e3gb_layer_norm_backward(R, C, x.data_ptr(), xs, xd, w, st, dy.data_ptr(), dys, dyd,
-                                                     dx.data_ptr(), dxs, dxd, pw, pb, pws, nws, s))
+                                                     dx.data_ptr(), dxs, dxd, pw, pb, pws, nws, _current(dev)))
     return dx, dw, db
 
 
@@ -775,6 +781,8 @@ def irreps_norm_forward(blocks, x, weight=None, bias=None, eps: float = 1e-5, ou
     take bias [number of even scalar blocks, mul]. Rotations and reflections commute with it. stats
     [N, n_blocks, 2] = (mean or 0, 1/rms) goes to the backward. y: float32, or `dtype`."""
     import torch
+    if stream is not None:
+        return _on(stream, irreps_norm_forward, blocks, x, weight, bias, eps, out, dtype, out=out)
     _, ir, scalars = _irreps_operand(blocks, x)
     shape, nb, dev, at, f = x.shape, len(blocks), x.device, x.get_device(), torch.float32
     N, _, mul = shape
@@ -784,9 +792,8 @@ def irreps_norm_forward(blocks, x, weight=None, bias=None, eps: float = 1e-5, ou
         _same_layout("y", y, x)
     xd, yd = _dtype_code("x", x), _dtype_code("y", y)
     stats = torch.empty((N, nb, 2), dtype=f, device=dev)
-    s = _current(dev) if stream is None else _given(stream, stats, y if out is None else None)
     _check((_lib or load()).e3gb_irreps_norm_forward(ir, N, x.data_ptr(), xd, w, b if scalars else None, eps, y.data_ptr(),
-                                                     yd, stats.data_ptr(), s))
+                                                     yd, stats.data_ptr(), _current(dev)))
     return y, stats
 
 
@@ -795,6 +802,8 @@ def irreps_norm_backward(blocks, x, weight, stats, dy, out=None, dtype=None, par
     """(dx, dweight, dbias) of irreps_norm_forward for the cotangent dy [N, d1, mul] and the
     forward's stats; dbias is None where there is no even scalar block. params=False: dx only."""
     import torch
+    if stream is not None:
+        return _on(stream, irreps_norm_backward, blocks, x, weight, stats, dy, out, dtype, params, workspace, out=out)
     key, ir, scalars = _irreps_operand(blocks, x)
     shape, nb, dev, at, f = x.shape, len(key), x.device, x.get_device(), torch.float32
     N, _, mul = shape
@@ -816,10 +825,8 @@ def irreps_norm_backward(blocks, x, weight, stats, dy, out=None, dtype=None, par
         if scalars:
             db = torch.empty((scalars, mul), dtype=f, device=dev)
             pb = db.data_ptr()
-    s = _current(dev) if stream is None else _given(stream, dw, db, ws if workspace is None else None,
-                                                    dx if out is None else None)
     _check((_lib or load()).e3gb_irreps_norm_backward(ir, N, x.data_ptr(), xd, w, st, dy.data_ptr(), dyd, dx.data_ptr(), dxd,
-                                                      pw, pb, pws, nws, s))
+                                                      pw, pb, pws, nws, _current(dev)))
     return dx, dw, db
 
 
@@ -967,14 +974,15 @@ def adamw_step(opt: AdamW, grads, lr: float, step: int, betas=(0.9, 0.999), eps:
     scaling is returned ([1] float32 on the device, else None), and a step whose norm is not finite
     changes nothing."""
     import torch
+    if stream is not None:
+        return _on(stream, lambda: (adamw_step(opt, grads, lr, step, betas, eps, max_norm),))[0]
     code, addresses = opt.gradient_addresses(grads)
     if max_norm is not None and not max_norm > 0:
         raise ValueError("max_norm must be positive")
     dev = opt.plan.device
     norm = None if max_norm is None else torch.empty(1, dtype=torch.float32, device=dev)
     rates = _AdamwRates(lr, betas[0], betas[1], eps, max_norm or 0.0, step, opt.seed)
-    s = _current(dev) if stream is None else _given(stream, norm)
-    ms, vs = opt.m_scale, opt.v_scale
+    s, ms, vs = _current(dev), opt.m_scale, opt.v_scale
     _check(_lib.e3gb_adamw_step(opt.handle, opt.plan.data_ptr(), addresses.buffer_info()[0], code, opt.m.data_ptr(), opt.v.data_ptr(),
                                 None if ms is None else ms.data_ptr(), None if vs is None else vs.data_ptr(),
                                 ctypes.byref(rates), None if norm is None else norm.data_ptr(),

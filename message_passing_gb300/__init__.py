@@ -13,7 +13,7 @@ from __future__ import annotations
 import array
 import ctypes
 import os
-from dataclasses import dataclass
+from dataclasses import dataclass, field
 from functools import lru_cache
 from operator import attrgetter
 
@@ -852,6 +852,7 @@ class AdamW:
     v_scale: object
     plan: object
     workspace: object
+    streams: set = field(default_factory=set)   # raw, on which the buffers are known to be in use
 
     @classmethod
     def create(cls, params, weight_decay=0.01, state_bits: int = 32, state=None, copies=None, seed: int = 0) -> "AdamW":
@@ -909,7 +910,19 @@ class AdamW:
             _shape(name, t, *s)
             _contig(t)
             setattr(a, name, t)
+        if dev.type == "cuda":
+            torch.cuda.current_stream(dev).synchronize()   # the first step may be on any stream
         return a
+
+    def keep_for(self, raw: int):
+        """Marks every buffer that the kernels read or write as used on the current stream (raw): a step may still
+        be queued there when the handle, perhaps the last holder of all of them, goes away."""
+        import torch
+        s = torch.cuda.current_stream(self.plan.device)
+        for t in (self.plan, self.workspace, self.m, self.v, self.m_scale, self.v_scale, *self.params, *self.copies):
+            if t is not None:
+                t.record_stream(s)
+        self.streams.add(raw)
 
     def gradient_addresses(self, grads):
         """(dtype code, array of addresses, 0 for None) of one step's gradients, checked against the
@@ -983,6 +996,8 @@ def adamw_step(opt: AdamW, grads, lr: float, step: int, betas=(0.9, 0.999), eps:
     norm = None if max_norm is None else torch.empty(1, dtype=torch.float32, device=dev)
     rates = _AdamwRates(lr, betas[0], betas[1], eps, max_norm or 0.0, step, opt.seed)
     s, ms, vs = _current(dev), opt.m_scale, opt.v_scale
+    if s not in opt.streams:
+        opt.keep_for(s)
     _check(_lib.e3gb_adamw_step(opt.handle, opt.plan.data_ptr(), addresses.buffer_info()[0], code, opt.m.data_ptr(), opt.v.data_ptr(),
                                 None if ms is None else ms.data_ptr(), None if vs is None else vs.data_ptr(),
                                 ctypes.byref(rates), None if norm is None else norm.data_ptr(),

@@ -37,3 +37,45 @@ def test_results_do_not_lie_in_memory_that_the_callers_stream_still_reads(cuda, 
     torch.cuda.synchronize()
     assert torch.all(late == 7.0)
     assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("how", ["given", "current"])
+def test_adamw_keeps_its_buffers_for_the_streams_of_its_steps(cuda, bits, how, monkeypatch):
+    """A handle that goes away after a step takes nothing with it that the step still needs: all that the kernel
+    addresses is marked as used on the step's stream, once."""
+    params = [torch.ones(700, device="cuda"), torch.ones(30, 10, device="cuda")]
+    copies = [None, torch.ones(30, 10, dtype=torch.bfloat16, device="cuda")]
+    grads = [torch.ones_like(p) for p in params]
+    opt = e3.AdamW.create(params, state_bits=bits, copies=copies)
+    torch.cuda.synchronize()
+    marked, real = [], torch.Tensor.record_stream
+    monkeypatch.setattr(torch.Tensor, "record_stream",
+                        lambda t, s: (marked.append((t.data_ptr(), s.cuda_stream)), real(t, s))[1])
+    s = torch.cuda.Stream()
+
+    def step(t):
+        if how == "given":
+            return e3.adamw_step(opt, grads, lr=1e-2, step=t, max_norm=1.0, stream=s)
+        with torch.cuda.stream(s):
+            return e3.adamw_step(opt, grads, lr=1e-2, step=t, max_norm=1.0)
+
+    step(1)
+    held = [opt.plan, opt.workspace, opt.m, opt.v, opt.m_scale, opt.v_scale, *params, copies[1]]
+    for t in held:
+        if t is not None:
+            assert (t.data_ptr(), s.cuda_stream) in marked
+    marked.clear()
+    step(2)
+    assert all(where != s.cuda_stream for _, where in marked)
+    torch.cuda.synchronize()
+
+
+def test_adamw_moments_are_ready_for_any_stream(cuda):
+    """create() returns when the moments it made are zero: a first step on another stream need not wait."""
+    big = torch.zeros(1 << 28, device="cuda")
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)
+    opt = e3.AdamW.create([big])
+    assert torch.cuda.current_stream().query()
+    del opt

@@ -663,6 +663,13 @@ def _on(stream, call, *args, out=None):
     return results
 
 
+def _written(*tensors):
+    """Raises the version counters of tensors that a call wrote by their addresses, so that autograd refuses a
+    backward pass that had saved one of them."""
+    import torch
+    torch.autograd.graph.increment_version([t for t in tensors if t is not None and not t.is_inference()])
+
+
 def _row_stride(name, t, at, R, C):
     """Entries between the rows of t [R, C], whose rows are contiguous and do not overlap, on device `at`."""
     if t.get_device() != at:
@@ -706,6 +713,8 @@ def layer_norm_forward(x, weight=None, bias=None, eps: float = 1e-5, out=None, d
     stats = torch.empty((R, 2), dtype=f, device=dev)
     _check((_lib or load()).e3gb_layer_norm_forward(R, C, x.data_ptr(), xs, xd, w, b, eps, y.data_ptr(), ys, yd,
                                                     stats.data_ptr(), _current(dev)))
+    if out is not None:
+        _written(out)
     return y, stats
 
 
@@ -735,6 +744,8 @@ def layer_norm_backward(x, weight, stats, dy, out=None, dtype=None, params: bool
         pw, pb, pws, nws = dw.data_ptr(), db.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size()
     _check((_lib or load()).e3gb_layer_norm_backward(R, C, x.data_ptr(), xs, xd, w, st, dy.data_ptr(), dys, dyd,
                                                      dx.data_ptr(), dxs, dxd, pw, pb, pws, nws, _current(dev)))
+    if out is not None:
+        _written(out)
     return dx, dw, db
 
 
@@ -794,6 +805,8 @@ def irreps_norm_forward(blocks, x, weight=None, bias=None, eps: float = 1e-5, ou
     stats = torch.empty((N, nb, 2), dtype=f, device=dev)
     _check((_lib or load()).e3gb_irreps_norm_forward(ir, N, x.data_ptr(), xd, w, b if scalars else None, eps, y.data_ptr(),
                                                      yd, stats.data_ptr(), _current(dev)))
+    if out is not None:
+        _written(out)
     return y, stats
 
 
@@ -827,6 +840,8 @@ def irreps_norm_backward(blocks, x, weight, stats, dy, out=None, dtype=None, par
             pb = db.data_ptr()
     _check((_lib or load()).e3gb_irreps_norm_backward(ir, N, x.data_ptr(), xd, w, st, dy.data_ptr(), dyd, dx.data_ptr(), dxd,
                                                       pw, pb, pws, nws, _current(dev)))
+    if out is not None:
+        _written(out)
     return dx, dw, db
 
 
@@ -853,6 +868,7 @@ class AdamW:
     plan: object
     workspace: object
     streams: set = field(default_factory=set)   # raw, on which the buffers are known to be in use
+    tracked: list = field(default_factory=list)   # what a step writes that has a version counter
 
     @classmethod
     def create(cls, params, weight_decay=0.01, state_bits: int = 32, state=None, copies=None, seed: int = 0) -> "AdamW":
@@ -910,6 +926,7 @@ class AdamW:
             _shape(name, t, *s)
             _contig(t)
             setattr(a, name, t)
+        a.tracked = [t for t in (*params, *copies, a.m, a.v, a.m_scale, a.v_scale) if t is not None and not t.is_inference()]
         if dev.type == "cuda":
             torch.cuda.current_stream(dev).synchronize()   # the first step may be on any stream
         return a
@@ -925,8 +942,8 @@ class AdamW:
         self.streams.add(raw)
 
     def gradient_addresses(self, grads):
-        """(dtype code, array of addresses, 0 for None) of one step's gradients, checked against the
-        parameters. With hundreds of tensors this is most of a step's time on the host, so the checks
+        """(dtype code, array of addresses, 0 for None, whether there is no None) of one step's gradients, checked
+        against the parameters. With hundreds of tensors this is most of a step's time on the host, so the checks
         run as maps over the whole list; the loop below finds out what is wrong, or skips None."""
         import torch
         T, n = torch.Tensor, len(self.params)
@@ -939,7 +956,7 @@ class AdamW:
                     and set(map(T.get_device, grads)) == {self.plan.get_device()}):
                 kind = kinds.pop()
                 if kind in codes:
-                    return codes[kind], array.array("Q", map(T.data_ptr, grads))
+                    return codes[kind], array.array("Q", map(T.data_ptr, grads)), True
         except (AttributeError, TypeError):
             pass                                   # a None among them
         kind, out = None, array.array("Q", bytes(8 * n))
@@ -956,7 +973,7 @@ class AdamW:
             if not g.is_contiguous():
                 raise ValueError(f"grads[{i}] must be contiguous")
             out[i] = g.data_ptr()
-        return codes.get(kind, F32), out
+        return codes.get(kind, F32), out, not any(g is None for g in grads)
 
     def moments(self, i: int):
         """(m, v) of tensor i as float32 tensors of its shape."""
@@ -989,7 +1006,7 @@ def adamw_step(opt: AdamW, grads, lr: float, step: int, betas=(0.9, 0.999), eps:
     import torch
     if stream is not None:
         return _on(stream, lambda: (adamw_step(opt, grads, lr, step, betas, eps, max_norm),))[0]
-    code, addresses = opt.gradient_addresses(grads)
+    code, addresses, every = opt.gradient_addresses(grads)
     if max_norm is not None and not max_norm > 0:
         raise ValueError("max_norm must be positive")
     dev = opt.plan.device
@@ -1002,6 +1019,11 @@ def adamw_step(opt: AdamW, grads, lr: float, step: int, betas=(0.9, 0.999), eps:
                                 None if ms is None else ms.data_ptr(), None if vs is None else vs.data_ptr(),
                                 ctypes.byref(rates), None if norm is None else norm.data_ptr(),
                                 opt.workspace.data_ptr(), opt.workspace.numel(), s))
+    if every:
+        torch.autograd.graph.increment_version(opt.tracked)
+    else:
+        given = [i for i, g in enumerate(grads) if g is not None]
+        _written(*(opt.params[i] for i in given), *(opt.copies[i] for i in given), opt.m, opt.v, ms, vs)
     return norm
 
 

@@ -663,6 +663,14 @@ def _on(stream, call, *args, out=None):
     return results
 
 
+def _apart(named):
+    """Refuses contiguous tensors [(name, tensor)] of which two share memory: a step writes all of them at once."""
+    spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), name) for name, t in named if t.numel())
+    for (_, end, a), (start, _, b) in zip(spans, spans[1:]):
+        if start < end:
+            raise ValueError(f"{a} and {b} share memory")
+
+
 def _written(*tensors):
     """Raises the version counters of tensors that a call wrote by their addresses, so that autograd refuses a
     backward pass that had saved one of them."""
@@ -875,7 +883,7 @@ class AdamW:
         """params: contiguous float32 device tensors. weight_decay: one number, or one for each
         tensor. state: (m, v) or (m, v, m_scale, v_scale) to use as the moments (zeros by default).
         copies: bfloat16 tensors (or None) that every step also writes the rounded parameters to.
-        seed: of the bits that round 8-bit moments."""
+        seed: of the bits that round 8-bit moments. No two of all these may share memory."""
         import torch
         params = [p.detach() for p in params]
         n = len(params)
@@ -895,9 +903,13 @@ class AdamW:
                     _elsewhere(f"copies[{i}]", c, at)
                 _shape(f"copies[{i}]", c, *p.shape)
                 _contig(c)
-        for name, t in zip(("m", "v", "m_scale", "v_scale"), state or ()):
+        moments = list(zip(("m", "v", "m_scale", "v_scale"), state or ()))
+        for name, t in moments:
             if t.get_device() != at:
                 _elsewhere(name, t, at)
+            _contig(t)
+        _apart([(f"params[{i}]", p) for i, p in enumerate(params)] + moments
+               + [(f"copies[{i}]", c) for i, c in enumerate(copies) if c is not None])
         lib = load()
         ptrs = lambda ts: (ctypes.c_void_p * n)(*[None if t is None else t.data_ptr() for t in ts])  # noqa: E731
         h = ctypes.c_void_p()
@@ -924,7 +936,6 @@ class AdamW:
             if t.dtype != d:
                 raise TypeError(f"{name} must be {d}")
             _shape(name, t, *s)
-            _contig(t)
             setattr(a, name, t)
         a.tracked = [t for t in (*params, *copies, a.m, a.v, a.m_scale, a.v_scale) if t is not None and not t.is_inference()]
         if dev.type == "cuda":

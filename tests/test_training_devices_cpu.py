@@ -74,3 +74,26 @@ def test_the_device_has_to_be_the_current_one(monkeypatch):
         e3._current(device(1))
     with pytest.raises(ValueError, match="expected device memory"):
         e3._current(torch.device("cpu"))
+
+
+BUF = torch.zeros(1024)
+
+
+@pytest.mark.parametrize("params,kw,names", [
+    ([W, X, W], {}, "params.0. and params.2."),
+    ([BUF[:100], BUF[200:300], BUF[99:120]], {}, "params.0. and params.2."),
+    ([BUF[300:500], BUF[200:301]], {}, "params.1. and params.0."),
+    ([W], dict(state=(BUF[:256], BUF[:256])), "m and v"),
+    ([BUF[:8]], dict(state=(BUF[:256], torch.zeros(256))), "m|params"),
+    ([torch.zeros(4), torch.zeros(4)], dict(copies=[torch.zeros(8, dtype=torch.bfloat16)[:4]] * 2), "copies.0. and copies.1."),
+    ([BUF[:8]], dict(copies=[BUF.view(torch.bfloat16)[14:22]]), "params.0. and copies.0."),
+])
+def test_tensors_that_share_memory(params, kw, names):
+    with pytest.raises(ValueError, match=f"({names}).* share memory"):
+        e3.AdamW.create(params, **kw)
+
+
+def test_neighbours_in_one_buffer_do_not_share_memory():
+    """Nor do tensors without entries; these are then refused as host memory only."""
+    with pytest.raises(e3.E3GBError, match="not device memory|cannot query"):
+        e3.AdamW.create([BUF[100:200], BUF[:100], BUF[200:], BUF[5:5], BUF[5:5]])

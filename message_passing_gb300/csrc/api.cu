@@ -6,6 +6,7 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <limits>
 #include <map>
 #include <tuple>
 #include <mutex>
@@ -966,8 +967,22 @@ e3gb_status e3gb_adamw_step(const e3gb_adamw* a, const void* plan, const void* c
         if (!(h.eps >= 1e-30 && h.eps < 1e30)) return fail(E3GB_ERR_INVALID_ARG, "eps must be positive");
         if (!(h.max_norm >= 0.0) || std::isinf(h.max_norm)) return fail(E3GB_ERR_INVALID_ARG, "max_norm must be finite and >= 0");
         if (h.step < 1) return fail(E3GB_ERR_INVALID_ARG, "step must be >= 1");
-        const int n = int(a->tensors.size());
         const bool clips = h.max_norm > 0.0;
+        AdamwRates r;
+        r.beta1 = float(h.beta1);
+        r.rest1 = float(1.0 - h.beta1);
+        r.beta2 = float(h.beta2);
+        r.rest2 = float(1.0 - h.beta2);
+        r.lr = float(h.lr);
+        r.step_size = float(h.lr / (1.0 - std::pow(h.beta1, double(h.step))));
+        r.root = float(1.0 / std::sqrt(1.0 - std::pow(h.beta2, double(h.step))));
+        r.eps = float(h.eps);
+        // a positive max_norm below fp32's numbers is its smallest one, not "no clipping"
+        r.max_norm = clips ? std::fmax(float(h.max_norm), std::numeric_limits<float>::denorm_min()) : 0.f;
+        r.key = adamw_key(h.seed, h.step);
+        if (!std::isfinite(r.lr) || !std::isfinite(r.step_size))
+            return fail(E3GB_ERR_INVALID_ARG, "lr, or lr / (1 - beta1^step), is above what fp32 holds");
+        const int n = int(a->tensors.size());
         for (int i = 0; i < n; ++i)
             if (reinterpret_cast<uintptr_t>(grads[i]) % elt_bytes(g_dtype) != 0)
                 return fail(E3GB_ERR_INVALID_ARG, "gradient %d is not %zu-byte aligned", i, elt_bytes(g_dtype));
@@ -981,17 +996,6 @@ e3gb_status e3gb_adamw_step(const e3gb_adamw* a, const void* plan, const void* c
         E3GB_TRY(check_ptr(v_scale, "v_scale", 4, any && eight));
         E3GB_TRY(check_ptr(norm_out, "norm_out", 4, clips));
         E3GB_TRY(check_ptr(workspace, "workspace", 16, clips));
-        AdamwRates r;
-        r.beta1 = float(h.beta1);
-        r.rest1 = float(1.0 - h.beta1);
-        r.beta2 = float(h.beta2);
-        r.rest2 = float(1.0 - h.beta2);
-        r.lr = float(h.lr);
-        r.step_size = float(h.lr / (1.0 - std::pow(h.beta1, double(h.step))));
-        r.root = float(1.0 / std::sqrt(1.0 - std::pow(h.beta2, double(h.step))));
-        r.eps = float(h.eps);
-        r.max_norm = float(h.max_norm);
-        r.key = adamw_key(h.seed, h.step);
         const AdamwTensor* tensors = static_cast<const AdamwTensor*>(plan);
         return cuda_status(adamw_step(tensors, reinterpret_cast<const int32_t*>(tensors + n), a->first_chunk.data(), n,
                                       grads, g_dtype == E3GB_BF16, {m, v, m_scale, v_scale, a->bits}, r, norm_out,

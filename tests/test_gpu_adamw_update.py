@@ -45,3 +45,14 @@ def test_adamw_decays_by_little(cuda, bits, lr, decay):
     want, _, _ = oracle.adamw.step(before, to_np(g), zero, zero, lr=lr, t=1, decay=wd)
     bound = U * np.abs(want) * (1 + 1e-6) + 16 * U * lr + 4 * U * lr * wd * np.abs(before)
     assert np.all(np.abs(to_np(p) - want) <= bound)
+
+
+def test_adamw_clips_by_less_than_fp32_holds(cuda):
+    """A max_norm of 1e-60 is one all the same: the norm comes back, and the gradients are scaled to nothing."""
+    p = _normal(5000, 5)
+    before, g = p.clone(), _normal(5000, 6)
+    opt = e3.AdamW.create([p], weight_decay=0.0)
+    norm = e3.adamw_step(opt, [g], lr=1e-2, step=1, max_norm=1e-60)
+    want = np.sqrt((to_np(g) ** 2).sum())
+    assert abs(float(norm) - want) <= 32 * U * want
+    assert torch.equal(p, before) and float(opt.m.abs().max()) < 1e-44

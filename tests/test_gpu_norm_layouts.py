@@ -50,3 +50,12 @@ def _case(R, C, dtype, offsets, strides, seed):
 def test_layer_norm_rows_that_begin_inside_a_vector(cuda, t, offset, R, C, stride):
     """All four tensors begin equally far into a vector, the first of a buffer too."""
     _case(R, C, t, [offset] * 4, [stride] * 4, seed=C + offset)
+
+
+@pytest.mark.parametrize("t", [F, B])
+@pytest.mark.parametrize("offsets,gaps", [((0, 1, 0, 2), (0, 0, 0, 0)), ((3, 0, 1, 0), (1, 2, 0, 3)), ((1, 1, 1, 1), (1, 1, 1, 2)),
+                                          ((0, 0, 0, 0), (5, 5, 5, 5)), ((2, 2, 2, 2), (3, 3, 7, 3)), ((0, 8, 0, 8), (8, 8, 0, 16))])
+@pytest.mark.parametrize("R,C", [(37, 5), (65, 64), (300, 77), (64, 128), (37, 130), (65, 700), (33, 2050), (330, 5001), (20, 9002)])
+def test_layer_norm_writes_only_its_rows_at_any_alignment(cuda, t, offsets, gaps, R, C):
+    """Tensors that lie over one another in vectors, or not: entries between and beside the rows keep their values."""
+    _case(R, C, t, offsets, [C + g for g in gaps], seed=C)

@@ -177,14 +177,13 @@ bool by_length(int64_t n, F&& f) {
     if constexpr (VEC == 8) {
         if (n <= 2) return f(Int<2>{}, Int<1>{}), true;
         if (n <= 4) return f(Int<4>{}, Int<1>{}), true;
-        if (n <= 8) return f(Int<4>{}, Int<2>{}), true;
-        if constexpr (ODD) {
-            if (n <= 12) return f(Int<4>{}, Int<3>{}), true;
+        if constexpr (!ODD) {   // odd rows of 5 to 64 vectors of eight go by vectors of four (wide_odd)
+            if (n <= 8) return f(Int<4>{}, Int<2>{}), true;
+            if (n <= 16) return f(Int<8>{}, Int<2>{}), true;
+            if (n <= 32) return f(Int<16>{}, Int<2>{}), true;
+            if (n <= 48) return f(Int<16>{}, Int<3>{}), true;
+            if (n <= 64) return f(Int<32>{}, Int<2>{}), true;
         }
-        if (n <= 16) return f(Int<8>{}, Int<2>{}), true;
-        if (n <= 32) return f(Int<16>{}, Int<2>{}), true;
-        if (n <= 48) return f(Int<16>{}, Int<3>{}), true;
-        if (n <= 64) return f(Int<32>{}, Int<2>{}), true;
         if (n <= 128) return f(Int<32>{}, Int<4>{}), true;
         if (n <= 256) return f(Int<256>{}, Int<1>{}), true;
         if (n <= 512) return f(Int<256>{}, Int<2>{}), true;

@@ -282,18 +282,25 @@ int flat_threads(int each) {
     return 32;
 }
 
-// Rows of a thread in shared memory: `want`, or what a block has room for. Two take the backward
-// kernels furthest (131,072 x 1024 bf16: 129 us with two, 141 with three, 150 with six; more take
-// from the L1 cache and from the registers), and the forward ones with few whole vectors a lane.
-// Blocks that share a row and hold little of it take three (31,250 x 4096 bf16, backward: 172 us with
-// two, 144 with three).
-// Rows of a lane's ring: two or three, as many as fit. Three keep wide rows' loads going while a row's sum
-// goes through its barrier; but where 512 lanes hold 3, 5, 6 or 8 vectors of four each, and forward 256
-// lanes 5, two are enough, and three take shared memory and registers that the loop needs (backward,
-// 10,666 x 6000 fp32: 141, 125 us; forward, 12,800 x 5000: 94, 78 us; with 4 vectors, 15,625 x 8192, two
-// cost 257 against 239 us).
-template <int VEC, int L, int NV>
-constexpr bool two_stages = VEC == 4 && L == 512 && NV != 4;
+// Rows of a lane's ring in shared memory: two or three. Three keep loads going while a row's sum goes through its
+// shuffles or its barrier, two leave the L1 cache and the registers more. Measured, 64M entries, with two and
+// with three:
+//   forward, three: bf16 by vectors of eight with three or more a lane (768: 55, 49 us; 1024: 48, 44; 264: 48, 43, but
+//     384: 42, 45) and bf16 of rows shared by warps (2048: 51, 47; 4096: 52, 46; 6000: 48, 44; to fp32 66, 61); odd
+//     rows of up to 256 lanes (fp32 77: 90, 83; 321: 90, 84; 1999: 87, 83);
+//   forward, two: other fp32 (64: 83, 86; 768: 78, 88; 2048: 77, 92; 5000: 78, 94; but 6000: 92, 83), and a warp with
+//     eight vectors (odd fp32 999: 88, 132);
+//   backward, three: rows of 256 lanes (fp32 4096: 127, 121; 5000: 131, 122; bf16 2048: 90, 84; 4096: 93, 79), bf16 by
+//     three or more vectors of eight (384: 69, 63; 768: 73, 72), fp32 by four vectors in 512 lanes (8192: 135,
+//     130; but 7000: 123, 135);
+//   backward, two: other rows (fp32 64: 126, 125; 512: 122, 125; 6000: 125, 141; bf16 16384: 114, 134) and odd ones
+//     (fp32 77: 119, 143; 3001: 179, 225; bf16 321: 119, 147; 5001: 147, 168; 13001: 187, 227).
+template <class TX, int VEC, int L, int NV, bool ODD>
+constexpr int forward_rows = (ODD ? L <= 256 && NV <= 4 : sizeof(TX) == 2 && (L > 32 || (VEC == 8 && NV >= 3))) ? 3 : 2;
+template <class TX, class TD, int VEC, int L, int NV, bool ODD>
+constexpr int backward_rows = !ODD && (L == 256 || (L <= 32 && VEC == 8 && NV >= 3) ||
+                                       (L == 512 && VEC == 4 && NV == 4 && sizeof(TX) + sizeof(TD) == 8)) ? 3 : 2;
+// as many of those as a block has room for
 constexpr int row_stages(int slot, int want) { return want * slot <= 216 * 1024 ? want : 2 * slot <= 216 * 1024 ? 2 : 1; }
 
 int resident(const void* kernel, int threads, int smem) { return grid_for(kernel, threads, 1, int64_t(1) << 40, smem); }
@@ -373,7 +380,7 @@ cudaError_t forward(const NormShape& sh, const TX* xc, const float* w, const flo
         constexpr bool ODD = decltype(odd)::value;
         return by_length<VEC, ODD>(vectors_of(sh.mul, VEC, ODD), [&](auto l, auto nv) {
             constexpr int L = decltype(l)::value, NV = decltype(nv)::value, T = segments::kThreads<L>;
-            constexpr int slot = segments::Ring<TX, VEC, L, NV, ODD>::kBytes, S = row_stages(slot, !two_stages<VEC, L, NV> && !(VEC == 4 && NV == 5) && ((L > 32 && sizeof(TX) == 2) || ODD || NV * VEC > 16) ? 3 : 2), smem = slot * S;
+            constexpr int slot = segments::Ring<TX, VEC, L, NV, ODD>::kBytes, S = row_stages(slot, forward_rows<TX, VEC, L, NV, ODD>), smem = slot * S;
             auto* k = segments::forward_kernel<TX, TY, VEC, L, NV, S, ODD>;
             e = allow_smem([] {}, (const void*)k);
             if (e != cudaSuccess) return;
@@ -464,7 +471,7 @@ cudaError_t backward(const NormShape& sh, const TX* xc, const float* w, const fl
             return by_length<VEC, ODD>(vectors_of(sh.mul, VEC, ODD), [&](auto l, auto nv) {
                 constexpr int L = decltype(l)::value, NV = decltype(nv)::value, T = segments::kThreads<L>;
                 constexpr int slot = segments::Ring<TX, VEC, L, NV, ODD>::kBytes + segments::Ring<TD, VEC, L, NV, ODD>::kBytes + 8 * T;
-                constexpr int S = row_stages(slot, !two_stages<VEC, L, NV> && L > 32 && (NV > 2 || sizeof(TX) + sizeof(TD) < 8) ? 3 : 2), smem = slot * S;
+                constexpr int S = row_stages(slot, backward_rows<TX, TD, VEC, L, NV, ODD>), smem = slot * S;
                 auto* k = segments::backward_kernel<TX, TD, TO, VEC, L, NV, S, ODD>;
                 e = allow_smem([] {}, (const void*)k);
                 if (e != cudaSuccess) return;

@@ -338,11 +338,20 @@ cudaError_t allow_smem(TAG, const void* kernel) {
 
 constexpr int64_t kL2Bytes = 126 * 1000 * 1000;
 
-// Irreps rows of 16 and 32 bytes whose inputs fit in the L2 cache are loaded as read once (100,000 x 16
-// x 8 fp32: forward 16.9 against 20.4 us, backward 31.5 against 33.5), larger ones are kept in the
-// caches (400,000: 71 against 83 and 100 against 131 us).
+// Irreps of 4 and 8 channels in fp32 (rows of 16 and 32 bytes) whose bytes stay in the L2 cache anyway are loaded as
+// read once, larger ones are kept in the caches. Measured, read once and kept:
+//   forward, 8 channels, up to what x and y hold together (120,000 x 16: 23, 26 us; 200,000 x 9: 25, 28; 50,000 x 31:
+//     17, 20; above, 150,000 x 16: 33, 31; 200,000 x 16: 44, 38; 250,000 x 9: 36, 34);
+//   forward, 4 channels, up to three quarters by x (400,000 x 9: 29, 32; 600,000 x 9: 45, 53; above, 800,000 x 9: 90, 73);
+//   backward, 8 channels, up to x and dy (75,000 x 16: 26, 29; 100,000 x 16: 31, 34; 200,000 x 9: 46, 49; above, 150,000
+//     x 16: 53, 46; 250,000 x 9: 58, 52).
 template <class TX, int VEC, int MV>
 constexpr bool read_once = VEC == 4 && MV <= 2 && sizeof(TX) == 4;
+template <class TX, class TY, int L, int MV>
+bool forward_once(int64_t entries) {
+    return MV < L ? entries * int64_t(sizeof(TX) + sizeof(TY)) <= kL2Bytes
+                  : entries * int64_t(sizeof(TX)) <= kL2Bytes / 4 * 3;
+}
 
 // Nodes, a multiple of unit between half of `about` and twice it, that share rows out most evenly among
 // thread blocks that take so many at a time.
@@ -411,7 +420,7 @@ cudaError_t forward(const NormShape& sh, const TX* xc, const float* w, const flo
             constexpr bool once = read_once<TX, VEC, MV>;
             if constexpr (blocks::kPairs<TX, TY, VEC, L, MV, CG>)
                 launch(blocks::irreps_forward_pairs_kernel<TX, TY, VEC, L, MV, CG>, 2);
-            else if (once && sh.rows * sh.x_stride * int64_t(sizeof(TX)) <= kL2Bytes)
+            else if (once && forward_once<TX, TY, L, MV>(sh.rows * sh.x_stride))
                 launch(blocks::irreps_forward_kernel<TX, TY, VEC, L, MV, CG, !once>, 1);
             else
                 launch(blocks::irreps_forward_kernel<TX, TY, VEC, L, MV, CG, true>, 1);

@@ -289,17 +289,18 @@ int flat_threads(int each) {
 //     384: 42, 45) and bf16 of rows shared by warps (2048: 51, 47; 4096: 52, 46; 6000: 48, 44; to fp32 66, 61); odd
 //     rows of up to 256 lanes (fp32 77: 90, 83; 321: 90, 84; 1999: 87, 83);
 //   forward, two: other fp32 (64: 83, 86; 768: 78, 88; 2048: 77, 92; 5000: 78, 94; but 6000: 92, 83), and a warp with
-//     eight vectors (odd fp32 999: 88, 132);
-//   backward, three: rows of 256 lanes (fp32 4096: 127, 121; 5000: 131, 122; bf16 2048: 90, 84; 4096: 93, 79), bf16 by
-//     three or more vectors of eight (384: 69, 63; 768: 73, 72), fp32 by four vectors in 512 lanes (8192: 135,
-//     130; but 7000: 123, 135);
-//   backward, two: other rows (fp32 64: 126, 125; 512: 122, 125; 6000: 125, 141; bf16 16384: 114, 134) and odd ones
-//     (fp32 77: 119, 143; 3001: 179, 225; bf16 321: 119, 147; 5001: 147, 168; 13001: 187, 227).
+//     eight vectors of four (odd fp32 999: 88, 132; bf16 to fp32 1024: 61, 66, but 700: 68, 63);
+//   backward, three: rows of 256 lanes (fp32 4096: 127, 121; 5000: 131, 122; bf16 2048: 90, 84; 4096: 93, 79) but for
+//     fp32 by two vectors (2048, 134M entries: 246, 259); fp32 by four vectors in 512 lanes (8192: 135, 130; but
+//     7000: 123, 135);
+//   backward, two: other rows (fp32 64: 126, 125; 512: 122, 125; 6000: 125, 141; bf16 1024, 134M entries: 126, 136;
+//     16384: 114, 134; but 384: 69, 63) and odd ones (fp32 77: 119, 143; 3001: 179, 225; bf16 321: 119, 147; 5001: 147,
+//     168; 13001: 187, 227).
 template <class TX, int VEC, int L, int NV, bool ODD>
 constexpr int forward_rows = (ODD ? L <= 256 && NV <= 4 : sizeof(TX) == 2 && (L > 32 || (VEC == 8 && NV >= 3))) ? 3 : 2;
 template <class TX, class TD, int VEC, int L, int NV, bool ODD>
-constexpr int backward_rows = !ODD && (L == 256 || (L <= 32 && VEC == 8 && NV >= 3) ||
-                                       (L == 512 && VEC == 4 && NV == 4 && sizeof(TX) + sizeof(TD) == 8)) ? 3 : 2;
+constexpr int backward_rows =
+    !ODD && (sizeof(TX) + sizeof(TD) < 8 ? L == 256 : (L == 256 && NV > 2) || (L == 512 && NV == 4)) ? 3 : 2;
 // as many of those as a block has room for
 constexpr int row_stages(int slot, int want) { return want * slot <= 216 * 1024 ? want : 2 * slot <= 216 * 1024 ? 2 : 1; }
 

@@ -876,7 +876,7 @@ class AdamW:
     plan: object
     workspace: object
     streams: set = field(default_factory=set)   # raw, on which the buffers are known to be in use
-    tracked: list = field(default_factory=list)   # what a step writes that has a version counter
+    tracked: list = field(default_factory=list)   # tensors whose version counters a step raises
 
     @classmethod
     def create(cls, params, weight_decay=0.01, state_bits: int = 32, state=None, copies=None, seed: int = 0) -> "AdamW":
@@ -885,6 +885,8 @@ class AdamW:
         copies: bfloat16 tensors (or None) that every step also writes the rounded parameters to.
         seed: of the bits that round 8-bit moments. No two of all these may share memory."""
         import torch
+        params, copies = list(params), None if copies is None else list(copies)
+        given = [t for t in (*params, *(copies or ())) if t is not None]
         params = [p.detach() for p in params]
         n = len(params)
         copies = [None] * n if copies is None else [c if c is None else c.detach() for c in copies]
@@ -937,7 +939,10 @@ class AdamW:
                 raise TypeError(f"{name} must be {d}")
             _shape(name, t, *s)
             setattr(a, name, t)
-        a.tracked = [t for t in (*params, *copies, a.m, a.v, a.m_scale, a.v_scale) if t is not None and not t.is_inference()]
+        # views of one buffer share its version counter
+        given += [t for t in (a.m, a.v, a.m_scale, a.v_scale) if t is not None]
+        counted = {id(b): b for b in (t if t._base is None else t._base for t in given)}
+        a.tracked = [t for t in counted.values() if not t.is_inference()]
         if dev.type == "cuda":
             torch.cuda.current_stream(dev).synchronize()   # the first step may be on any stream
         return a

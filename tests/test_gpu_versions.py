@@ -52,3 +52,15 @@ def test_inference_tensors_have_no_version(cuda):
     r = torch.randn(5, 8, device="cuda")
     y, _ = e3.layer_norm_forward(r, out=out)
     assert torch.equal(y, e3.layer_norm_forward(r)[0]) and float(p.max()) < 1.0
+
+
+def test_parameters_that_are_views_of_one_buffer(cuda):
+    """They share the buffer's version counter, also with other views of it."""
+    buf = torch.zeros(1000, device="cuda")
+    params = [buf[100 * i:100 * i + 60] for i in range(4)] + [torch.nn.Parameter(buf[500:600])]
+    opt = e3.AdamW.create(params)
+    other, grads = buf[600:], [torch.ones_like(p) for p in params]
+    for step in (1, 2):
+        before = [t._version for t in (*params, other, buf)]
+        e3.adamw_step(opt, grads, lr=1e-2, step=step)
+        assert all(t._version > v for t, v in zip((*params, other, buf), before))

@@ -854,6 +854,12 @@ def irreps_norm_backward(blocks, x, weight, stats, dy, out=None, dtype=None, par
 
 
 _GET_DTYPE = attrgetter("dtype")
+_MOMENTS = ("m", "v", "m_scale", "v_scale")
+
+
+def _named(params, copies):
+    return ([(f"params[{i}]", p) for i, p in enumerate(params)]
+            + [(f"copies[{i}]", c) for i, c in enumerate(copies) if c is not None])
 
 
 @dataclass
@@ -861,11 +867,12 @@ class AdamW:
     """AdamW handle (e3gb_adamw) over float32 parameters, which it updates where they lie: they must
     keep their storage while the handle lives. m, v: the moments of all tensors in one buffer each,
     tensor i's from entry starts[i]; float32, or with state_bits=8 float8_e4m3fn and float8_e5m2 with a
-    power-of-two scale (m_scale, v_scale) for each 256 entries: saved and restored as any tensors."""
+    power-of-two scale (m_scale, v_scale) for each 256 entries: saved and restored as any tensors, also by
+    setting one of the four attributes (to a tensor of the same type, shape and device)."""
     handle: ctypes.c_void_p
-    params: list
+    params: tuple
     numel: tuple
-    copies: list
+    copies: tuple
     state_bits: int
     seed: int
     starts: list
@@ -877,6 +884,8 @@ class AdamW:
     workspace: object
     streams: set = field(default_factory=set)   # raw, on which the buffers are known to be in use
     tracked: list = field(default_factory=list)   # tensors whose version counters a step raises
+    given: tuple = ()                             # the parameters and copies as create() got them
+    kinds: dict | None = None                     # shape and type of each moment, once create() is done
 
     @classmethod
     def create(cls, params, weight_decay=0.01, state_bits: int = 32, state=None, copies=None, seed: int = 0) -> "AdamW":
@@ -885,11 +894,11 @@ class AdamW:
         copies: bfloat16 tensors (or None) that every step also writes the rounded parameters to.
         seed: of the bits that round 8-bit moments. No two of all these may share memory."""
         import torch
-        params, copies = list(params), None if copies is None else list(copies)
-        given = [t for t in (*params, *(copies or ())) if t is not None]
-        params = [p.detach() for p in params]
+        params = tuple(params)
         n = len(params)
-        copies = [None] * n if copies is None else [c if c is None else c.detach() for c in copies]
+        copies = (None,) * n if copies is None else tuple(copies)
+        given = tuple(t for t in params + copies if t is not None)
+        params, copies = tuple(p.detach() for p in params), tuple(c if c is None else c.detach() for c in copies)
         decay = [float(weight_decay)] * n if isinstance(weight_decay, (int, float)) else [float(d) for d in weight_decay]
         if n < 1 or len(copies) != n or len(decay) != n:
             raise ValueError(f"{n} parameters, {len(copies)} copies, {len(decay)} weight decays")
@@ -905,13 +914,12 @@ class AdamW:
                     _elsewhere(f"copies[{i}]", c, at)
                 _shape(f"copies[{i}]", c, *p.shape)
                 _contig(c)
-        moments = list(zip(("m", "v", "m_scale", "v_scale"), state or ()))
+        moments = list(zip(_MOMENTS, state or ()))
         for name, t in moments:
             if t.get_device() != at:
                 _elsewhere(name, t, at)
             _contig(t)
-        _apart([(f"params[{i}]", p) for i, p in enumerate(params)] + moments
-               + [(f"copies[{i}]", c) for i, c in enumerate(copies) if c is not None])
+        _apart(_named(params, copies) + moments)
         lib = load()
         ptrs = lambda ts: (ctypes.c_void_p * n)(*[None if t is None else t.data_ptr() for t in ts])  # noqa: E731
         h = ctypes.c_void_p()
@@ -934,18 +942,45 @@ class AdamW:
                      for s, d in want]
         if len(state) != len(want):
             raise ValueError(f"state of {len(state)} tensors, expected {len(want)}")
-        for name, t, (s, d) in zip(("m", "v", "m_scale", "v_scale"), state, want):
-            if t.dtype != d:
-                raise TypeError(f"{name} must be {d}")
-            _shape(name, t, *s)
+        kinds = dict(zip(_MOMENTS, want))
+        for name, t in zip(_MOMENTS, state):
+            a._fits(name, t, kinds)
             setattr(a, name, t)
-        # views of one buffer share its version counter
-        given += [t for t in (a.m, a.v, a.m_scale, a.v_scale) if t is not None]
-        counted = {id(b): b for b in (t if t._base is None else t._base for t in given)}
-        a.tracked = [t for t in counted.values() if not t.is_inference()]
+        a.given, a.kinds = given, kinds
+        a._track()
         if dev.type == "cuda":
             torch.cuda.current_stream(dev).synchronize()   # the first step may be on any stream
         return a
+
+    def __setattr__(self, name, value):
+        if name not in _MOMENTS or self.kinds is None:
+            return object.__setattr__(self, name, value)
+        self._fits(name, value, self.kinds)
+        others = [(k, t) for k, t in self._moments() if k != name]
+        _apart(_named(self.params, self.copies) + others + [(name, value)])
+        object.__setattr__(self, name, value)
+        self.streams = set()
+        self._track()
+
+    def _moments(self):
+        return [(k, getattr(self, k)) for k in _MOMENTS if getattr(self, k) is not None]
+
+    def _fits(self, name, t, kinds):
+        if name not in kinds:
+            raise ValueError(f"moments of {self.state_bits} bits have no {name}")
+        shape, dtype = kinds[name]
+        if t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}")
+        if t.get_device() != self.plan.get_device():
+            _elsewhere(name, t, self.plan.get_device())
+        _shape(name, t, *shape)
+        _contig(t)
+
+    def _track(self):
+        """Views of one buffer share its version counter."""
+        held = [*self.given, *(t for _, t in self._moments())]
+        counted = {id(b): b for b in (t if t._base is None else t._base for t in held)}
+        self.tracked = [t for t in counted.values() if not t.is_inference()]
 
     def keep_for(self, raw: int):
         """Marks every buffer that the kernels read or write as used on the current stream (raw): a step may still

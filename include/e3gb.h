@@ -364,7 +364,9 @@ e3gb_status e3gb_layer_norm_backward(int64_t rows, int64_t cols, const void *x, 
  *   even scalars (l = 0, parity +1):  y = (x - mu) s w + b, mu and s over the mul channels;
  *   other blocks:                     y = x s w, s = 1/sqrt(sum x^2 / ((2l+1) mul) + eps).
  * weight [n_blocks][mul], bias [number of even scalar blocks][mul] (fp32, or NULL);
- * stats [nodes][n_blocks][2] = (mu, s), mu = 0 where there is no mean. */
+ * stats [nodes][n_blocks][2] = (mu, s), mu = 0 where there is no mean. A NaN, or an infinity in an
+ * even scalar block, gives NaN in all of its block of that node only; an infinity in another block
+ * gives s = 0, NaN in that entry and zeros beside it (and NaN in all of the block's dx). */
 e3gb_status e3gb_irreps_norm_forward(const e3gb_irreps *irreps, int64_t nodes, const void *x,
                                      e3gb_dtype x_dtype, const float *weight, const float *bias,
                                      float eps, void *y, e3gb_dtype y_dtype, float *stats,
@@ -404,10 +406,18 @@ e3gb_status e3gb_adamw_plan(const e3gb_adamw *a, void *plan);
  *   p = p (1 - lr decay) - lr / (1 - beta1^t) m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
  * max_norm > 0 scales every g by min(1, max_norm / norm) first, norm being the 2-norm of all
  * gradients, which is written to norm_out (device fp32); if it is not finite, nothing but
- * norm_out is written. 8-bit moments are rounded at random, by bits that depend on (seed, t,
- * entry) only; the update uses them before rounding; a moment that is not finite becomes NaN.
- * grads is a host array, read before the call returns. The workspace is used with max_norm > 0
- * only (16-byte aligned). Deterministic. */
+ * norm_out is written. Squares are taken in fp32: a gradient above 1.8e19 makes the norm infinite,
+ * one below 1e-23 counts as zero in it; at beta2 = 0.999 a first step's v loses bits for gradients
+ * below 3e-18 and is zero below 1e-21.
+ * 1 - lr decay is held in 48 bits and p rounded once; the root and the reciprocal in the update are
+ * the hardware's approximations, each within two units of 2^-24, subnormal v included.
+ * 8-bit moments are rounded at random, by bits that depend on (seed, t, entry) only; the update
+ * uses them before rounding; a moment that is not finite becomes NaN. Their scales are at least
+ * 2^-71 (m) and 2^-78 (v), so that a stored v is at least 2^-94 where it is not zero.
+ * eps is in 1e-30..1e30; lr and lr / (1 - beta1^t) have to be numbers that fp32 holds.
+ * grads is a host array, read before the call returns; the addresses in it have to be device memory
+ * of the tensors' sizes (they are not queried, as other pointers are: there may be hundreds).
+ * The workspace is used with max_norm > 0 only (16-byte aligned). Deterministic. */
 typedef struct {
     double lr, beta1, beta2, eps, max_norm;
     int64_t step;

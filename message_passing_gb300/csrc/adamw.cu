@@ -21,7 +21,7 @@
 // moments and bf16 gradients. A thread block takes a run of neighbouring chunks of 4096 entries.
 // Measured: 134M entries, fp32 gradients, bf16 copies and clipping 711 us (the step itself 96% of the
 // copy rate, the norm's second read of the gradients 100 us); 200M entries with 8-bit moments and
-// bf16 gradients 457 us (91%; the arithmetic units are 60-70% busy, so the loads have to come early).
+// bf16 gradients 458 us (91%; the arithmetic units are 60-70% busy, so the loads have to come early).
 #include "adamw.cuh"
 #include "async_copy.cuh"
 

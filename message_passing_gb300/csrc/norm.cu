@@ -171,7 +171,7 @@ using Bool = std::integral_constant<bool, V>;
 
 // f(L, NV) for rows of n vectors. Returns false where a row is too long for registers. Many steps from 256
 // lanes on: with lanes for the next power of two, a row of 5001 fp32 took 123 us forward and 245 backward
-// (64M entries), one of 9001 193 and 289; with these 107, 158 and 95, 145.
+// (64M entries), one of 9001 193 and 289; with these 107, 161 and 95, 146.
 template <int VEC, bool ODD, class F>
 bool by_length(int64_t n, F&& f) {
     if constexpr (VEC == 8) {
@@ -373,7 +373,7 @@ segments::Tensor<T> rows_of(T* p, int64_t stride, const NormShape& sh) {
 }
 
 // Whether odd bf16 rows of n entries go by vectors of eight: between these bounds vectors of four waste
-// fewer lanes on the two ends (backward, 64M entries: 117 against 143 us at 77, 120 against 152 at 999).
+// fewer lanes on the two ends (backward, 64M entries, by eight and by four: 143, 117 us at 77; 120, 152 at 999).
 bool wide_odd(int64_t n) { return n < 24 || n > 512; }
 
 // vectors that a row of n entries can touch

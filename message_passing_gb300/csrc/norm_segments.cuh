@@ -6,14 +6,14 @@
 // on one; mean, variance and output come from the registers. A lane's channels are the same in every
 // row that it takes, so that it sums its part of dw and db over all of them; one partial sum per
 // thread block goes to memory. Measured, of the copy rate: forward 2.56M x 64 bf16 107 us (93%),
-// backward 131,072 x 1024 bf16 126 us (95%), 1M x 128 fp32 163 us (93%) and 237 us (96%).
+// backward 131,072 x 1024 bf16 127 us (94%), 1M x 128 fp32 162 us (93%) and 236 us (96%).
 //
 // Rows that are not whole vectors (ODD): a row's first entry then lies `shift` entries into a vector,
 // and shift depends on the row modulo VEC only. A lane group's rows are a multiple of VEC apart, so
 // that its channels still are the same in all of them; the vectors at the two ends hold entries of
 // the rows beside, which are masked, and are written entry by entry. Rows of more than about 70
-// entries reach 80-95% of the copy rate in fp32 (50,021 x 321, backward: 36 us, 79%); in bf16, and
-// narrower, the masks and the lanes past the end make the instructions the bound (40-60%).
+// entries reach 70-95% of the copy rate in fp32 (50,021 x 321, backward: 36 us, 78%; 701 columns 53%); in bf16, and
+// narrower, the masks and the lanes past the end make the instructions the bound (39-60%).
 #pragma once
 #include "async_copy.cuh"
 #include "norm.cuh"

@@ -663,12 +663,16 @@ def _on(stream, call, *args, out=None):
     return results
 
 
-def _apart(named):
-    """Refuses contiguous tensors [(name, tensor)] of which two share memory: a step writes all of them at once."""
-    spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), name) for name, t in named if t.numel())
+def _apart(params, copies, moments):
+    """Refuses contiguous tensors of which two share memory: a step writes all of them at once. moments: [(name,
+    tensor)]."""
+    tensors = [*params, *copies, *(t for _, t in moments)]
+    spans = sorted((t.data_ptr(), t.data_ptr() + t.nbytes, k) for k, t in enumerate(tensors) if t is not None and t.numel())
+    n = len(params)
+    name = lambda k: (f"params[{k}]" if k < n else f"copies[{k - n}]" if k < 2 * n else moments[k - 2 * n][0])  # noqa: E731
     for (_, end, a), (start, _, b) in zip(spans, spans[1:]):
         if start < end:
-            raise ValueError(f"{a} and {b} share memory")
+            raise ValueError(f"{name(a)} and {name(b)} share memory")
 
 
 def _written(*tensors):
@@ -857,11 +861,6 @@ _GET_DTYPE = attrgetter("dtype")
 _MOMENTS = ("m", "v", "m_scale", "v_scale")
 
 
-def _named(params, copies):
-    return ([(f"params[{i}]", p) for i, p in enumerate(params)]
-            + [(f"copies[{i}]", c) for i, c in enumerate(copies) if c is not None])
-
-
 @dataclass
 class AdamW:
     """AdamW handle (e3gb_adamw) over float32 parameters, which it updates where they lie: they must
@@ -919,7 +918,7 @@ class AdamW:
             if t.get_device() != at:
                 _elsewhere(name, t, at)
             _contig(t)
-        _apart(_named(params, copies) + moments)
+        _apart(params, copies, moments)
         lib = load()
         ptrs = lambda ts: (ctypes.c_void_p * n)(*[None if t is None else t.data_ptr() for t in ts])  # noqa: E731
         h = ctypes.c_void_p()
@@ -949,7 +948,9 @@ class AdamW:
         a.given, a.kinds = given, kinds
         a._track()
         if dev.type == "cuda":
-            torch.cuda.current_stream(dev).synchronize()   # the first step may be on any stream
+            here = torch.cuda.current_stream(dev)
+            here.synchronize()                  # the first step may be on any stream
+            a.streams = {here.cuda_stream}      # what was allocated here needs no mark for it
         return a
 
     def __setattr__(self, name, value):
@@ -957,7 +958,7 @@ class AdamW:
             return object.__setattr__(self, name, value)
         self._fits(name, value, self.kinds)
         others = [(k, t) for k, t in self._moments() if k != name]
-        _apart(_named(self.params, self.copies) + others + [(name, value)])
+        _apart(self.params, self.copies, others + [(name, value)])
         object.__setattr__(self, name, value)
         self.streams = set()
         self._track()
